@@ -391,7 +391,9 @@ mxfp4_status mxfp4_qema_quantize(const uint16_t *w, int64_t R, int64_t C, int64_
  * 128-block, so that a product's tile reads a block's scales contiguously.
  * Codes between k and k rounded up to 128 are zeros (every quantizer here
  * writes them), so k may be anything.  A view is a descriptor with larger ld
- * or scale_ld.
+ * or scale_ld.  Of each line of scales the `rows` bytes of the matrix are read
+ * (a product reads them in aligned words of four, and between a view's lines
+ * whatever the wider matrix holds there): the last line's memory may end with them.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int64_t rows;

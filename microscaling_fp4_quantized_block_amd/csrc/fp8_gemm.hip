@@ -193,10 +193,11 @@ __device__ __forceinline__ void fp8_mainloop(const Fp8Args& p, uint8_t* smem, in
   const Share sb1 = make_share<32>(p.b, n0 + lb0 + (GATED ? p.np : BH), p.kb);
   const Lanes la = make_lanes(p.a.ld, l), lb = make_lanes(p.b.ld, l);
   // scale bytes: even waves bring A's 256 rows, odd waves B's, 4 per lane.
-  // Rows past the matrix read whatever lies there or, past its end, zeros.
+  // Rows past the matrix read the next line's bytes or, past the last line's
+  // last row, zeros.
   const Fp8In& so = (w & 1) ? p.b : p.a;
   const int64_t s0 = (w & 1) ? n0 : m0;
-  const __amdgpu_buffer_rsrc_t sres = resource(so.scales + s0, (int64_t)p.kb * so.scale_ld - s0);
+  const __amdgpu_buffer_rsrc_t sres = resource(so.scales + s0, fp8_scale_extent(p.kb, so.scale_ld, so.rows, s0, 4));
   const uint32_t soff = 4 * l + ((GATED && (w & 1) && l >= 32) ? (uint32_t)(p.np - 128) : 0u);
   const uint32_t sld = (uint32_t)so.scale_ld;
   auto stage = [&](int a) { return smem + (a & 1) * F8_STAGE; };
@@ -605,11 +606,11 @@ __global__ void __launch_bounds__(64 * DEC_NW) fp8_decode_kernel(Fp8Args p) {
     int64_t rows = p.b.rows - first;
     rows = rows < 0 ? 0 : rows > 16 ? 16 : rows;
     bt[j].codes = resource(p.b.codes + (rows ? first : 0) * p.b.ld, rows ? (rows - 1) * p.b.ld + kp : 0);
-    bt[j].scales = resource(p.b.scales + (rows ? first : 0), rows ? (int64_t)p.kb * p.b.scale_ld - first : 0);
+    bt[j].scales = resource(p.b.scales + (rows ? first : 0), fp8_scale_extent(p.kb, p.b.scale_ld, p.b.rows, first, 1));
   }
   Rows16 at;
   at.codes = resource(p.a.codes + m0 * p.a.ld, (rows_a - 1) * p.a.ld + kp);
-  at.scales = resource(p.a.scales + m0, (int64_t)p.kb * p.a.scale_ld - m0);
+  at.scales = resource(p.a.scales + m0, fp8_scale_extent(p.kb, p.a.scale_ld, p.a.rows, m0, 1));
   uint8_t* const ring = smem + w * (R * SLOT);
 
   // load q of a slot moves slot rows 8 q .. + 7 (weight rows first); lane l

@@ -22,6 +22,15 @@ struct Fp8In {
   int64_t rows;
 };
 
+// Bytes that a product may read from line 0's scale of row `first` of an
+// operand, over its kb lines: up to the last line's own last row, in loads of
+// `unit` bytes at multiples of it (lines and operands start at multiples of
+// 16).  A view's lines start inside those of a wider matrix, whose memory may end
+// with the view's last row, a whole line pitch before that of a full matrix.
+constexpr int64_t fp8_scale_extent(int64_t kb, int64_t scale_ld, int64_t rows, int64_t first, int unit) {
+  return kb > 0 && first < rows ? (kb - 1) * scale_ld + (rows + unit - 1) / unit * unit - first : 0;
+}
+
 struct GatedGradArgs {
   const uint16_t *dh, *g, *u;
   int64_t ldd, ldg, ldu;
