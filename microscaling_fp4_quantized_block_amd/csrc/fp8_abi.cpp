@@ -16,8 +16,8 @@ using mxfp4::Fp8Out;
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// Rows and columns: a grid of 128 x 128 tiles (or of 16 rows x 512 columns)
-// stays below 2^31 workgroups, and sizes below stay below 2^63.
+// Rows and columns: sizes below stay below 2^63.  (One launch does not hold
+// every grid of 128 x 128 tiles: see in_parts and decode_tiles.)
 constexpr int64_t kMaxSide = (int64_t)1 << 30;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 // Operands of the products: 128 rows of codes, and all scales, are reached

@@ -845,9 +845,10 @@ static double reduce_time(int64_t M, int64_t N, int splits) {
 // 128 x 4096 x 14336 38.7 and 27.9; gated 64 x 4096 x 4096 15.9 and 30.5, 256 x
 // 1024 x 8192 19.2 and 50.1, 64 x 14336 x 4096 46.5 and 37.2.  (With more rows it
 // would still be for narrow outputs, 400 x 1024 x 8192 18.6 and 28.2, and not
-// for others, 400 x 4096 x 4096 35.3 and 26.5: those are left to the wide tiles.)
+// for others, 400 x 4096 x 4096 35.3 and 26.5: those are left to the wide tiles,
+// as are outputs of more columns than one launch of this kernel holds.)
 static int decode_tiles(int64_t M, int64_t N, int64_t kb, bool gated, double wide) {
-  if (M > 256) return 0;
+  if (M > 256 || ceil_div(N, gated ? 16 : 32) > FP8_LAUNCH_THREADS / (64 * DEC_NW)) return 0;
   const DecodeTime d = decode_time(M, N, kb, gated);
   return M <= 32 || d.us < wide ? d.tiles : 0;
 }

@@ -22,6 +22,10 @@ struct Fp8In {
   int64_t rows;
 };
 
+// A launch holds fewer than 2^32 threads along x: more are cut off without an
+// error just past it, and refused further on.
+constexpr int64_t FP8_LAUNCH_THREADS = ((int64_t)1 << 32) - 1;
+
 // Bytes that a product may read from line 0's scale of row `first` of an
 // operand, over its kb lines: up to the last line's own last row, in loads of
 // `unit` bytes at multiples of it (lines and operands start at multiples of

@@ -319,17 +319,41 @@ static void launch_tile(const uint16_t* x, int64_t R, int64_t C, int64_t ldx, in
     hipLaunchKernelGGL((fp8_tile_kernel<true, false, RAGGED>), grid, wg, 0, s, x, R, C, ldx, tc, out);
 }
 
+// f(first row, rows, first column, columns) for parts of [R, C] of which each
+// takes one launch: workgroups of `threads` (at most 512) for tr x tc elements
+// (at least 16 x 128).  Parts start at multiples of 128.
+template <typename F>
+static void in_parts(int64_t R, int64_t C, int64_t tr, int64_t tc, int64_t threads, F f) {
+  constexpr int64_t COLS = (int64_t)1 << 26;
+  const int64_t most = FP8_LAUNCH_THREADS / threads;
+  for (int64_t c0 = 0; c0 < C; c0 += COLS) {
+    const int64_t cols = C - c0 < COLS ? C - c0 : COLS;
+    const int64_t rows = most / ((cols + tc - 1) / tc) * tr / 128 * 128;
+    for (int64_t r0 = 0; r0 < R; r0 += rows) f(r0, R - r0 < rows ? R - r0 : rows, c0, cols);
+  }
+}
+
 hipError_t launch_fp8_quantize(const uint16_t* x, int64_t R, int64_t C, int64_t ldx, int axis, int block_rows,
                                const Fp8Out& out, hipStream_t s) {
+  auto part = [&](int64_t r0, int64_t c0) {
+    return axis ? Fp8Out{out.codes + r0 * out.ld + c0, out.scales + c0 / FP8_BLOCK * out.scale_ld + r0, out.ld, out.scale_ld}
+                : Fp8Out{out.codes + c0 * out.ld + r0, out.scales + r0 / FP8_BLOCK * out.scale_ld + c0, out.ld, out.scale_ld};
+  };
   if (axis == 1 && block_rows == 1) {
-    const int64_t blocks = (C + 127) / 128, groups = (blocks + ROWS_NB - 1) / ROWS_NB;
-    const int64_t n = groups * ((R + 15) / 16);
-    hipLaunchKernelGGL(fp8_rows_kernel, dim3((unsigned)n), dim3(256), 0, s, x, R, C, ldx, blocks, groups, out);
+    in_parts(R, C, 16, ROWS_NB * FP8_BLOCK, 256, [&](int64_t r0, int64_t rows, int64_t c0, int64_t cols) {
+      const int64_t blocks = (cols + 127) / 128, groups = (blocks + ROWS_NB - 1) / ROWS_NB;
+      const int64_t n = groups * ((rows + 15) / 16);
+      hipLaunchKernelGGL(fp8_rows_kernel, dim3((unsigned)n), dim3(256), 0, s, x + r0 * ldx + c0, rows, cols, ldx, blocks,
+                         groups, part(r0, c0));
+    });
     return hipGetLastError();
   }
-  const int64_t tc = (C + 127) / 128, n = tc * ((R + 127) / 128);
-  if (C % 8) launch_tile<true>(x, R, C, ldx, axis, block_rows, tc, out, n, s);
-  else launch_tile<false>(x, R, C, ldx, axis, block_rows, tc, out, n, s);
+  in_parts(R, C, 128, 128, TILE_THREADS, [&](int64_t r0, int64_t rows, int64_t c0, int64_t cols) {
+    const int64_t tc = (cols + 127) / 128, n = tc * ((rows + 127) / 128);
+    const uint16_t* p = x + r0 * ldx + c0;
+    if (C % 8) launch_tile<true>(p, rows, cols, ldx, axis, block_rows, tc, part(r0, c0), n, s);
+    else launch_tile<false>(p, rows, cols, ldx, axis, block_rows, tc, part(r0, c0), n, s);
+  });
   return hipGetLastError();
 }
 
