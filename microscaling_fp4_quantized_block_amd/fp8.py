@@ -7,6 +7,7 @@ and their gradients.  Layouts, formulas and errors are those of
 from __future__ import annotations
 
 import ctypes
+from operator import attrgetter
 from typing import Optional
 
 import torch
@@ -63,9 +64,11 @@ class Fp8Tensor:
     scales: uint8 [k / 128 rounded up, >= rows]
     pair:   for two matrices in one (the gated block's weights, the columns
             each has, or the rows): their own length; each is padded to 128
-    Rows may be strided by multiples of 16 bytes; both live on one GPU.
+    Rows may be strided by multiples of 16 bytes; both live on one GPU.  The
+    library reads a descriptor made from the fields, so they cannot be set again.
     """
-    __slots__ = ("rows", "k", "codes", "scales", "pair", "device", "_struct")
+    __slots__ = ("_rows", "_k", "_codes", "_scales", "pair", "_device", "_struct")
+    rows, k, codes, scales, device = (property(attrgetter(f)) for f in ("_rows", "_k", "_codes", "_scales", "_device"))
 
     def __init__(self, rows: int, k: int, codes: torch.Tensor, scales: torch.Tensor, pair: Optional[int] = None):
         kp, blocks = _up(k, 128), _up(k, 128) // 128
@@ -88,8 +91,8 @@ class Fp8Tensor:
         self._set(rows, k, codes, scales, pair, ld, scale_ld)
 
     def _set(self, rows, k, codes, scales, pair, ld, scale_ld):
-        self.rows, self.k, self.codes, self.scales, self.pair = rows, k, codes, scales, pair
-        self.device = codes.device
+        self._rows, self._k, self._codes, self._scales, self.pair = rows, k, codes, scales, pair
+        self._device = codes.device
         self._struct = Fp8TensorStruct(rows, k, ld, scale_ld, codes.data_ptr() or None, scales.data_ptr() or None)
 
     def elements(self) -> torch.Tensor:
