@@ -6,7 +6,8 @@
     out = h Wd^T                            (mxfp4_fp8_gemm)
 
 FeedForward.decode() serves single tokens: three calls, nothing but the weights
-read from memory.  FeedForward.train() is the same block under autograd:
+read from memory once serve() has laid those out.  FeedForward.train() is the
+same block under autograd:
 
     d(out) -> FP8 along its rows and along the tokens
     dh  = d(out) Wd,  dWd = d(out)^T h      (mxfp4_fp8_gemm)
@@ -65,23 +66,25 @@ class FeedForward:
         self.norm = torch.ones(width, dtype=torch.bfloat16, device=device).requires_grad_()
         self.gate, self.up, self.down = weight(hidden, width), weight(hidden, width), weight(width, hidden)
         self.act, self.eps = act, eps
-        self.served = None
 
     def parameters(self):
         return [self.norm, self.gate, self.up, self.down]
 
     def train(self, x, residual):
         """(out, r), differentiable in x, residual and the weights."""
-        self.served = None
         return _Block.apply(x, residual, self.norm, self.gate, self.up, self.down, self.act, self.eps)
 
     @torch.no_grad()
-    def decode(self, x, residual):
-        """(out, r); residual is overwritten with r.  The FP8 weights are laid out on the first call after a change."""
-        if self.served is None:
-            self.served = (mx.mxfp4_fp8_quantize_pair(self.gate, self.up),
-                           mx.mxfp4_fp8_quantize(self.down, block_rows=128))
-        pair, down = self.served
+    def serve(self):
+        """The products' weights as they are now, laid out in FP8: what a program keeps between decode() calls for as
+        long as it does not change them."""
+        return (mx.mxfp4_fp8_quantize_pair(self.gate, self.up), mx.mxfp4_fp8_quantize(self.down, block_rows=128))
+
+    @torch.no_grad()
+    def decode(self, x, residual, served=None):
+        """(out, r); residual is overwritten with r.  served: the weights of serve(); without them the weights are laid
+        out in the call."""
+        pair, down = served or self.serve()
         q, r = mx.mxfp4_fp8_rmsnorm(x, self.norm, self.eps, residual=residual, sum_out=residual)
         return mx.mxfp4_fp8_gemm(mx.mxfp4_fp8_gated(q, pair, act=self.act), down), r
 
@@ -107,10 +110,11 @@ def main():
     block = FeedForward(4096, 14336)
     x = torch.randn(1, 4096, device="cuda").to(torch.bfloat16)
     res = torch.zeros(1, 4096, dtype=torch.bfloat16, device="cuda")
-    block.decode(x, res)
+    served = block.serve()
+    block.decode(x, res, served)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        block.decode(x, res)
+        block.decode(x, res, served)
     for _ in range(10):
         graph.replay()
     torch.cuda.synchronize()
