@@ -230,7 +230,11 @@ def mxfp4_fp8_gemm_workspace_bytes(A: Fp8Tensor, B: Fp8Tensor) -> int:
 
 def mxfp4_fp8_gemm(A: Fp8Tensor, B: Fp8Tensor, dtype: torch.dtype = torch.bfloat16,
                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """C = A B^T [A.rows, B.rows], summed in binary32, as float32 or bfloat16."""
+    """C = A B^T [A.rows, B.rows] as float32 or bfloat16, accumulated in binary32
+    registers by a matrix instruction that cuts products to 13 binary places
+    below the largest of eight neighbours (include/mxfp4.h has the bound): float32
+    results are good to about 1.5e-5 of the root of the sum of their squared
+    products, where a binary32 product would be good to 1e-7."""
     _fp8(A, "A")
     _fp8(B, "B", device=A.device)
     if out is not None:
@@ -333,8 +337,8 @@ def mxfp4_fp8_gated_workspace_bytes(x: Fp8Tensor, w: Fp8Tensor, fp8_out: bool = 
 def mxfp4_fp8_gated(x: Fp8Tensor, w: Fp8Tensor, act: str = "silu", train: bool = False, dtype=None, out=None,
                     workspace: Optional[torch.Tensor] = None):
     """h = act(x Wg^T) * (x Wu^T) [x.rows, n], w the pair of weights: as an
-    Fp8Tensor (quantized from binary32), or in bf16 with
-    dtype=torch.bfloat16.  train=True: (h, g, u), the two projections in bf16 for
+    Fp8Tensor (quantized from binary32; the projections are as exact as
+    mxfp4_fp8_gemm's sums), or in bf16 with dtype=torch.bfloat16.  train=True: (h, g, u), the two projections in bf16 for
     the backward pass."""
     _fp8(x, "x")
     _fp8(w, "w", device=x.device)
