@@ -16,6 +16,7 @@ from . import _check, _nbytes, lib
 
 # the current stream's handle of a device index (torch.cuda.current_stream() builds a Stream object, 2 us a call)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _empty = torch.empty_strided   # (a quarter less host time a call than torch.empty)
 
 _byref = ctypes.byref
@@ -159,6 +160,16 @@ def _room(need: int, workspace: Optional[torch.Tensor], device):
     return workspace, _nbytes(workspace, device)
 
 
+def _launch(device: torch.device, f, *args) -> None:
+    """f(*args, stream) on the device's current stream.  Kernels go to the current device (the default stream's
+    handle is the same on all of them), which may be another one than the operands'."""
+    if device.index == _current_device():
+        _check(f(*args, _raw_stream(device.index)))
+    else:
+        with torch.cuda.device(device):
+            _check(f(*args, _raw_stream(device.index)))
+
+
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -180,8 +191,7 @@ def mxfp4_fp8_quantize(x: torch.Tensor, axis: int = 1, block_rows: int = 1,
         out = empty_fp8(rows, k, x.device)
     else:
         _fp8(out, "out", rows, k, x.device)
-    _check(lib.mxfp4_fp8_quantize(x.data_ptr(), R, C, ldx, int(axis), int(block_rows), _byref(out._struct),
-                                  _raw_stream(x.device.index)))
+    _launch(x.device, lib.mxfp4_fp8_quantize, x.data_ptr(), R, C, ldx, int(axis), int(block_rows), _byref(out._struct))
     return out
 
 
@@ -218,7 +228,7 @@ def mxfp4_fp8_dequantize(q: Fp8Tensor) -> torch.Tensor:
     """The binary32 values of q [rows, k]."""
     _fp8(q, "q")
     y = torch.empty((q.rows, q.k), dtype=torch.float32, device=q.device)
-    _check(lib.mxfp4_fp8_dequantize(_byref(q._struct), _p(y), max(q.k, 1), _raw_stream(q.device.index)))
+    _launch(q.device, lib.mxfp4_fp8_dequantize, _byref(q._struct), _p(y), max(q.k, 1))
     return y
 
 
@@ -247,8 +257,8 @@ def mxfp4_fp8_gemm(A: Fp8Tensor, B: Fp8Tensor, dtype: torch.dtype = torch.bfloat
     else:
         ldc = _matrix(out, "out", (A.rows, B.rows), A.device, dtype)
     ws, ws_bytes = _room(mxfp4_fp8_gemm_workspace_bytes(A, B), workspace, A.device)
-    _check(lib.mxfp4_fp8_gemm(_byref(A._struct), _byref(B._struct), out.data_ptr(), ldc, C_TYPE[dtype], _p(ws), ws_bytes,
-                              _raw_stream(A.device.index)))
+    _launch(A.device, lib.mxfp4_fp8_gemm, _byref(A._struct), _byref(B._struct), out.data_ptr(), ldc, C_TYPE[dtype],
+            _p(ws), ws_bytes)
     return out
 
 
@@ -278,8 +288,8 @@ def mxfp4_fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
         _fp8(out, "out", T, H, dev)
     y = _empty(shape, (H, 1), dtype=torch.bfloat16, device=dev) if train else None
     rstd = _empty((T,), (1,), dtype=torch.float32, device=dev) if train else None
-    _check(lib.mxfp4_fp8_rmsnorm(x.data_ptr(), T, H, ldx, _p(residual), ldr, weight.data_ptr(), eps,
-                                 _byref(out._struct), _p(sum_out), lds, _p(y), H, _p(rstd), _raw_stream(dev.index)))
+    _launch(dev, lib.mxfp4_fp8_rmsnorm, x.data_ptr(), T, H, ldx, _p(residual), ldr, weight.data_ptr(), eps,
+            _byref(out._struct), _p(sum_out), lds, _p(y), H, _p(rstd))
     r = x if residual is None else sum_out
     return (out, r, y, rstd) if train else (out, r)
 
@@ -309,9 +319,8 @@ def mxfp4_fp8_rmsnorm_backward(dy: torch.Tensor, r: torch.Tensor, weight: torch.
         ldx = _matrix(out, "out", shape, dev)
     dw = _empty((H,), (1,), dtype=torch.float32, device=dev)
     ws, ws_bytes = _room(mxfp4_fp8_rmsnorm_backward_workspace_bytes(T, H), workspace, dev)
-    _check(lib.mxfp4_fp8_rmsnorm_backward(dy.data_ptr(), T, H, ldd, r.data_ptr(), ldr, weight.data_ptr(),
-                                          rstd.data_ptr(), _p(dres), lde, out.data_ptr(), ldx, dw.data_ptr(), _p(ws),
-                                          ws_bytes, _raw_stream(dev.index)))
+    _launch(dev, lib.mxfp4_fp8_rmsnorm_backward, dy.data_ptr(), T, H, ldd, r.data_ptr(), ldr, weight.data_ptr(),
+            rstd.data_ptr(), _p(dres), lde, out.data_ptr(), ldx, dw.data_ptr(), _p(ws), ws_bytes)
     return out, dw
 
 
@@ -356,9 +365,9 @@ def mxfp4_fp8_gated(x: Fp8Tensor, w: Fp8Tensor, act: str = "silu", train: bool =
     g = torch.empty((T, n), dtype=torch.bfloat16, device=dev) if train else None
     u = torch.empty((T, n), dtype=torch.bfloat16, device=dev) if train else None
     ws, ws_bytes = _room(mxfp4_fp8_gated_workspace_bytes(x, w, fp8), workspace, dev)
-    _check(lib.mxfp4_fp8_gated(_byref(x._struct), _byref(w._struct), n, _act(act),
-                               _byref(out._struct) if fp8 else None, None if fp8 else out.data_ptr(), ldh,
-                               _p(g), _p(u), n, _p(ws), ws_bytes, _raw_stream(dev.index)))
+    _launch(dev, lib.mxfp4_fp8_gated, _byref(x._struct), _byref(w._struct), n, _act(act),
+            _byref(out._struct) if fp8 else None, None if fp8 else out.data_ptr(), ldh, _p(g), _p(u), n, _p(ws),
+            ws_bytes)
     return (out, g, u) if train else out
 
 
@@ -395,8 +404,8 @@ def mxfp4_fp8_gated_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor,
     dw = torch.empty((2 * np_, H), dtype=dtype, device=dev)
     ht = empty_fp8(n, T, dev) if want_ht else None
     ws, ws_bytes = _room(mxfp4_fp8_gated_backward_workspace_bytes(T, wt, xt), workspace, dev)
-    _check(lib.mxfp4_fp8_gated_backward(dh.data_ptr(), ldd, g.data_ptr(), u.data_ptr(), ldgu, T, n, _act(act), _byref(wt._struct),
-                                        _byref(xt._struct), _p(dx), max(H, 1), _p(dw), max(H, 1), C_TYPE[dtype],
-                                        _byref(ht._struct) if want_ht else None, _p(ws), ws_bytes, _raw_stream(dev.index)))
+    _launch(dev, lib.mxfp4_fp8_gated_backward, dh.data_ptr(), ldd, g.data_ptr(), u.data_ptr(), ldgu, T, n, _act(act),
+            _byref(wt._struct), _byref(xt._struct), _p(dx), max(H, 1), _p(dw), max(H, 1), C_TYPE[dtype],
+            _byref(ht._struct) if want_ht else None, _p(ws), ws_bytes)
     got = (dx, dw[:n], dw[np_:np_ + n])
     return got + (ht,) if want_ht else got
