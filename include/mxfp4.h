@@ -486,7 +486,8 @@ mxfp4_status mxfp4_fp8_gated(const mxfp4_fp8_tensor *x, const mxfp4_fp8_tensor *
  *   dg = dh u act'(g), du = dh act(g), each quantized to FP8 along its rows and
  *   along its columns, then
  *   dx [T, H] = dg Wg + du Wu  (bf16),   dw [2 np, H] = (dg^T x, du^T x)
- * (dw_type; rows n .. np - 1 of either half are zeros), H = the width of x.
+ * (dw_type; rows n .. np - 1 of either half are zeros, NaN where a column of x
+ * holds a NaN), H = the width of x.
  * wt: the transposed weights side by side, [H, 2 np] -- Wg^T in columns
  * 0 .. n - 1, Wu^T in columns np .. np + n - 1, zero codes between.  xt: x
  * quantized along the tokens, [H, T].  ht: NULL, or the FP8 transpose [n, T]

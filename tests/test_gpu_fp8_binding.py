@@ -28,3 +28,23 @@ def test_gated_backward_of_rows_wants_one_stride():
     dh, g, u, wt, xt, *_ = backward_case(mx, 2, 200, 130, "silu", 302)
     with pytest.raises(ValueError, match="row stride"):
         mx.mxfp4_fp8_gated_backward(to_device_bf16(dh), to_device_bf16(g), to_device_bf16(u, 3), wt, xt)
+
+
+def test_gated_backward_rows_that_pad_the_weights():
+    """Rows n .. np - 1 of either half of dw: zeros, and NaN only in the columns of x that hold one."""
+    mx = need_gpu()
+    T, H, n = 300, 200, 130
+    dh, g, u, wt, xt, *_ = backward_case(mx, T, H, n, "gelu", 303)
+    args = [to_device_bf16(t) for t in (dh, g, u)]
+    say("fp8 gated backward, padding rows")
+    for bad in (None, 7):
+        if bad is not None:
+            xt.scales[1, bad] = 255
+        dwg = mx.mxfp4_fp8_gated_backward(*args, wt, xt, act="gelu")[1]
+        dw = torch.as_strided(dwg, (512, H), (H, 1), 0)   # (both halves, 256 rows each)
+        for half in (dw[:256], dw[256:]):
+            keep = torch.ones(H, dtype=torch.bool, device="cuda")
+            if bad is not None:
+                keep[bad] = False
+            assert not half[n:, keep].any() and bool(torch.isfinite(half[:, keep]).all())
+            assert bool(torch.isnan(half[:, ~keep]).all())
