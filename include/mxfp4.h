@@ -450,7 +450,7 @@ mxfp4_status mxfp4_fp8_gemm(const mxfp4_fp8_tensor *A, const mxfp4_fp8_tensor *B
  * residual and sum (r is written there; it may be x or residual itself)
  * are both given or both NULL.  y (the norm in bf16) and rstd [T] are what a
  * backward pass needs; either may be NULL.  H <= 32768 (UNSUPPORTED_SHAPE
- * otherwise), eps >= 0.  No workspace. */
+ * otherwise), eps >= 0.  T = 0 or H = 0 writes nothing.  No workspace. */
 mxfp4_status mxfp4_fp8_rmsnorm(const uint16_t *x, int64_t T, int64_t H, int64_t ldx, const uint16_t *residual,
                                int64_t ldr, const uint16_t *weight, float eps, mxfp4_fp8_tensor *out, uint16_t *sum,
                                int64_t lds, uint16_t *y, int64_t ldy, float *rstd, hipStream_t stream);

@@ -384,7 +384,8 @@ def mxfp4_fp8_gated_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor,
     """(dx, dwg, dwu) of mxfp4_fp8_gated for bf16 dh [T, n]: g and u from the
     forward pass, wt the weights transposed (mxfp4_fp8_quantize_pair, axis=0), xt
     the input quantized along the tokens (mxfp4_fp8_quantize, axis=0).  dx is
-    bf16, dwg and dwu [n, H] are of dtype (float32 or bfloat16).  want_ht=True:
+    bf16, dwg and dwu [n, H] are of dtype (float32 or bfloat16; their sums are as
+    exact as mxfp4_fp8_gemm's).  want_ht=True:
     the FP8 transpose [n, T] of h too, which the down projection's weight
     gradient multiplies."""
     ldd = _matrix(dh, "dh")
